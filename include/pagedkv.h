@@ -404,14 +404,17 @@ size_t paged_cross_attention_workspace_size(int num_seqs, int num_q_tokens, int 
  *
  * For row r of sequence i and head j (KV head j / (num_heads / num_kv_heads)):
  *   out[r, j] = sum_t softmax_t(scale <query[r, j], K[t]>) V[t], t < seq_lens[i];
- * zeros where seq_lens[i] is 0. A value that is not finite makes its column of the
- * sequence's rows not finite (NaN where its weight is 0 in a row, or in the part of
- * the sum that the row's result is put together from). Rows outside every sequence's
+ * zeros where seq_lens[i] is 0. A row is NaN where one of its scores is NaN or +inf,
+ * or where all are -inf (a query or key that is not finite); a token of score -inf has
+ * weight 0. A value that is not finite makes its column of the sequence's rows not
+ * finite (NaN where its weight is 0 in a row, or in the part of the sum that the row's
+ * result is put together from). Rows outside every sequence's
  * range are left as they were. head_dim 64 or 128, block_size 8/16/32, cache_dtype = q_dtype or
  * PKV_FP8_E4M3. The call keeps no state: calls (and replays of captured ones) may
  * overlap where their outputs and workspaces do not, and the same inputs give the
  * same bits. Rounding: scores and sums in fp32, softmax weights rounded to the
- * cache's type (f16 for E4M3, where the query is rounded to f16 as well).
+ * cache's type (f16 for E4M3, where the query is rounded to f16 as well: a bf16
+ * element of 65,520 and more becomes infinite, and its row NaN).
  * Errors: PKV_ERR_SHAPE, PKV_ERR_UNSUPPORTED, PKV_ERR_DTYPE, PKV_ERR_NULL,
  * PKV_ERR_ALIGN, PKV_ERR_WORKSPACE, PKV_ERR_CUDA.
  */

@@ -43,11 +43,13 @@ namespace {
 
 // kWarps warps per (token, head) row, each taking every kWarps-th of its parts
 // (pieces x copies): out = sum_k w_k o_k / sum_k w_k, w_k = 2^(lse_k - max lse);
-// zeros for a sequence without tokens. A warp has eight parts in flight, their
-// log-sum-exps and rows together (a running maximum rescales the sums), so a row of
-// up to eight costs one memory latency; a row of more is given a block of its own
-// (one warp for each of 448 rows of 296 parts took 60 us). Launched before the main
-// kernel has ended (programmatic dependent launch); it finds its row meanwhile.
+// zeros for a sequence without tokens. A part of log-sum-exp -inf (no token of it has
+// a weight) drops out; a NaN one makes the row NaN, as do parts that are all -inf. A
+// warp has eight parts in flight, their log-sum-exps and rows together (a running
+// maximum rescales the sums), so a row of up to eight costs one memory latency; a row
+// of more is given a block of its own (one warp for each of 448 rows of 296 parts took
+// 60 us). Launched before the main kernel has ended (programmatic dependent launch); it
+// finds its row meanwhile.
 constexpr int kJoinWarps = 8;
 template <typename OT, int D, int kWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefillParams p) {
@@ -86,16 +88,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefillPara
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, lse[i]);
-    if (mx == -INFINITY) continue;
-    const float keep = fast_exp2(m - mx);
+    for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, lse[i]);  // a NaN is passed over here ..
+    const float sub = mx == -INFINITY ? 0.f : mx;
+    const float keep = fast_exp2(m - sub);
     m = mx;
     den *= keep;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= keep;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = fast_exp2(lse[i] - mx);
+      const float w = fast_exp2(lse[i] - sub);  // .. and reaches the sums here
       den += w;
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[i][v], acc[v]);
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefillPara
       for (int v = 0; v < V; ++v) acc[v] = fmaf(w, sums[x][lane * V + v], acc[v]);
     }
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = n > 0 ? 1.f / den : 0.f;  // den 0: 0 * inf
   OT* dst = static_cast<OT*>(p.out) + row * D + lane * V;
   float a, b;
   if constexpr (V == 4) {

@@ -701,14 +701,17 @@ __global__ void __launch_bounds__(kThreads, MINB)
           float mx = -INFINITY;
 #pragma unroll
           for (int x = 0; x < kConsumerWarps; ++x) mx = fmaxf(mx, rm[x * H + lane]);
+          // Cross attention: a piece whose scores are all -inf has no weight in its
+          // unit (a zero row, log-sum-exp -inf) instead of making it NaN.
+          const float sub = RAG && mx == -INFINITY ? 0.f : mx;
           float lsum = 0.f;
 #pragma unroll
           for (int x = 0; x < kConsumerWarps; ++x) {
-            const float wt = fast_exp2(rm[x * H + lane] - mx);
+            const float wt = fast_exp2(rm[x * H + lane] - sub);
             merge_scratch[lane * 8 + x] = wt;
             lsum = fmaf(wt, rl[x * H + lane], lsum);
           }
-          merge_scratch[lane * 8 + 4] = vscale / lsum;
+          merge_scratch[lane * 8 + 4] = RAG && !whole && lsum == 0.f ? 0.f : vscale / lsum;
           if (!whole) {
             const int64_t rowp = (int64_t)own_piece_slot(d.range, seg) * g + lane;
             prm.ws_lse[rowp] = mx + fast_log2(lsum);

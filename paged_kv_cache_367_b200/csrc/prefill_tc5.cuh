@@ -1362,19 +1362,24 @@ __global__ void __launch_bounds__(Cfg5<D, F8, KIND>::kThreads,
       float l0, l1;
       asm("mov.b64 {%0, %1}, %2;" : "=f"(l0), "=f"(l1) : "l"(prev_lsum));
       const float lsum = l0 + l1;
-      const float inv = lsum > 0.f ? vsc / lsum : 0.f;
+      // Cross attention: a row sum of 0 with tokens seen is a row whose scores are all
+      // -inf, NaN by the formula; as a part of one it has no weight (log-sum-exp -inf).
+      // A NaN sum stays NaN either way.
+      const bool cut = X && (REP > 1 || p.pieces > 1);
+      const float inv = lsum > 0.f || (X && !cut) ? vsc / lsum : 0.f;
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) {
         float o[64];
         tmem_ld64(tO + 64 * q, o);  // two loads in flight, one wait
-        if (X && (REP > 1 || p.pieces > 1)) {
+        if (cut) {
           if (prev_valid) {
             float* part = p.ws_o + prev_part * D + 64 * q;
 #pragma unroll
             for (int u = 0; u < 64; u += 4)
               *reinterpret_cast<float4*>(part + u) =
                   make_float4(o[u] * inv, o[u + 1] * inv, o[u + 2] * inv, o[u + 3] * inv);
-            if (q == 0) p.ws_lse[prev_part] = lsum > 0.f ? prev_m + fast_log2(lsum) : -INFINITY;
+            // A sum of 0 comes with prev_m -inf, and gives -inf.
+            if (q == 0) p.ws_lse[prev_part] = prev_m + fast_log2(lsum);
           }
         } else if (!F8 && prev_valid && out32) {
           // 16-bit caches: 32 bytes (a whole sector) per store when the output
