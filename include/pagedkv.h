@@ -389,7 +389,9 @@ size_t paged_cross_attention_workspace_size(int num_seqs, int num_q_tokens, int 
  *   query, out   [num_q_tokens, num_heads, head_dim], q_dtype (BF16/F16)
  *   query_start  [num_seqs + 1] int32, device: rows query_start[i] ..
  *                query_start[i+1]-1 are sequence i's queries (none, one, many: one
- *                token per sequence, the beams of a request, a prompt)
+ *                token per sequence, the beams of a request, a prompt). A sequence
+ *                without queries may hold any length and block ids: they are not
+ *                looked up
  *   seq_lens     [num_seqs] int32, device: sequence i's cached tokens, any number,
  *                independent of its queries; their K/V appended with paged_kv_append
  *   k_cache, v_cache, block_table, k_scale, v_scale, scale

@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  SegmentWalker walker;
-  init_walker<T, !RAG>(prm, *sched, walker);  // ends with __syncthreads
+  SegmentWalkerOf<RAG> walker;
+  init_walker<T>(prm, *sched, walker);  // ends with __syncthreads
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = prm.num_heads, Hkv = prm.num_kv_heads, group = Hq / Hkv, bs = prm.block_size;

@@ -94,6 +94,33 @@ __host__ __device__ __forceinline__ int load_len(const int32_t* p) {
 #endif
 }
 
+// The lengths a schedule is made from: one query per sequence, or (RAG: cross
+// attention) a sequence without queries counted as empty, so that its blocks are
+// neither read nor looked up.
+template <bool RAG>
+struct Lengths {
+  const int32_t* seq_lens;
+  __host__ __device__ int raw(int i) const { return load_len(seq_lens + i); }
+};
+template <>
+struct Lengths<true> {
+  const int32_t* seq_lens;
+  const int32_t* query_start;
+  int num_q_tokens;
+  __host__ __device__ int raw(int i) const {
+    const int q1 = load_len(query_start + i + 1), q0 = load_len(query_start + i);
+    const int L = load_len(seq_lens + i);
+    return (q0 > 0 ? q0 : 0) < (q1 < num_q_tokens ? q1 : num_q_tokens) ? L : 0;
+  }
+};
+template <bool RAG>
+__device__ __forceinline__ Lengths<RAG> lengths_of(const DecodeParams& prm) {
+  if constexpr (RAG)
+    return {prm.seq_lens, prm.query_start, prm.num_q_tokens};
+  else
+    return {prm.seq_lens};
+}
+
 // The cut of [0, W) into G static ranges over [0, Ws) and Rd dynamic ranges
 // over [Ws, W) (Rd = 0 means Ws = W).
 struct Cuts {
@@ -167,8 +194,8 @@ __host__ __device__ void for_each_piece(const Cuts& cu, int64_t P, int64_t first
 // range (a "head"), else first; the walk from the range's start stops short of
 // it. Pieces, whose partials need merging, thus come before whole units, and a
 // range ends on work that needs no merge.
-struct SegmentWalker {
-  const int32_t* seq_lens;
+template <bool RAG>
+struct SegmentWalkerOf : Lengths<RAG> {
   int S, Hkv, cap, cost, round;
   int64_t P;     // partition size, kNoSplit when the unit is never cut
   Cuts cuts;
@@ -201,7 +228,7 @@ struct SegmentWalker {
         p = 0;
         if (i < S) {
           L = clamp_len(Lnext, cap);
-          Lnext = i + 1 < S ? load_len(seq_lens + i + 1) : 0;
+          Lnext = i + 1 < S ? this->raw(i + 1) : 0;
         }
         continue;
       }
@@ -235,11 +262,13 @@ struct SegmentWalker {
     return false;
   }
 };
+using SegmentWalker = SegmentWalkerOf<false>;
 
 // Sets up `w` for the range [lo, hi): `fi`/`fbase`/`fL` locate the sequence
 // holding offset lo (fi < 0: empty range), `li`/`lbase`/`lL` the one holding
 // hi - 1, and `fLnext` is the raw length of sequence fi + 1.
-__host__ __device__ __forceinline__ void start_range(SegmentWalker& w, int64_t lo, int64_t hi,
+template <bool RAG>
+__host__ __device__ __forceinline__ void start_range(SegmentWalkerOf<RAG>& w, int64_t lo, int64_t hi,
                                                      int fi, int64_t fbase, int fL, int fLnext,
                                                      int li, int64_t lbase, int lL) {
   w.hi = hi;
@@ -321,7 +350,7 @@ struct SchedShared {
   int64_t f_base, l_base, d_base;
   Cuts cuts;
   int f_i, l_i, d_i;
-  int lens[kInitLens];  // raw seq_lens, in the one-pass set-up
+  int lens[kInitLens];  // raw lengths, in the one-pass set-up
 };
 
 // Zero rows of sequence i if it is empty and this CTA owns it (i % G == c).
@@ -353,9 +382,10 @@ __device__ __forceinline__ void mark_range_seqs(SchedShared& sh, int i, int64_t 
 // must call it; ends with __syncthreads), leaves the cuts in sh.cuts and the
 // sequence holding the start of the dynamic ranges in sh.d_i / sh.d_base. Also
 // zero-fills the output rows of zero-length sequences i with
-// i % gridDim.x == blockIdx.x (kZeroEmpty).
-template <typename OT, bool kZeroEmpty = true>
-__device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWalker& w) {
+// i % gridDim.x == blockIdx.x (not RAG, whose rows are found by query_range).
+template <typename OT, bool RAG = false>
+__device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWalkerOf<RAG>& w) {
+  const Lengths<RAG> lengths = lengths_of<RAG>(prm);
   const int S = prm.num_seqs, Hkv = prm.num_kv_heads, cap = prm.len_cap, cost = prm.unit_cost;
   const int round = prm.unit_round;
   const int G = gridDim.x, c = blockIdx.x;
@@ -370,10 +400,10 @@ __device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWal
     // One pass: each thread holds one sequence; a single scan gives both the
     // total work and every sequence's work offset.
     const int i = threadIdx.x;
-    const int raw = i < S ? __ldg(prm.seq_lens + i) : 0;
+    const int raw = i < S ? lengths.raw(i) : 0;
     const int L = clamp_len(raw, cap);
     if (i < S) sh.lens[i] = raw;
-    if (kZeroEmpty) zero_empty_rows<OT>(prm, i, L, G, c);
+    if (!RAG) zero_empty_rows<OT>(prm, i, L, G, c);
     const int64_t wi = i < S ? (int64_t)Hkv * unit_work(L, cost, round) : 0;
     const int64_t incl = block_inclusive_scan(wi, sh.scan, W);  // syncs: defaults above are set
     cu = make_cuts(W, G, prm.dyn_ranges, prm.static_share);
@@ -392,9 +422,9 @@ __device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWal
     // Pass 1: total work; zero rows of empty sequences.
     int64_t sum = 0;
     for (int i = threadIdx.x; i < S; i += blockDim.x) {
-      const int L = clamp_len(__ldg(prm.seq_lens + i), cap);
+      const int L = clamp_len(lengths.raw(i), cap);
       sum += (int64_t)Hkv * unit_work(L, cost, round);
-      if (kZeroEmpty) zero_empty_rows<OT>(prm, i, L, G, c);
+      if (!RAG) zero_empty_rows<OT>(prm, i, L, G, c);
     }
     block_inclusive_scan(sum, sh.scan, W);
     cu = make_cuts(W, G, prm.dyn_ranges, prm.static_share);
@@ -410,7 +440,7 @@ __device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWal
     int64_t carry = 0;
     for (int i0 = 0; i0 < S; i0 += blockDim.x) {
       const int i = i0 + threadIdx.x;
-      const int L = i < S ? clamp_len(__ldg(prm.seq_lens + i), cap) : 0;
+      const int L = i < S ? clamp_len(lengths.raw(i), cap) : 0;
       const int64_t wi = (int64_t)Hkv * unit_work(L, cost, round);
       int64_t chunk_tot;
       const int64_t incl = block_inclusive_scan(wi, sh.scan, chunk_tot);
@@ -425,7 +455,7 @@ __device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWal
     }
     __syncthreads();
   }
-  w.seq_lens = prm.seq_lens;
+  static_cast<Lengths<RAG>&>(w) = lengths;
   w.S = S;
   w.Hkv = Hkv;
   w.cap = cap;
@@ -435,7 +465,7 @@ __device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWal
   w.cuts = cu;
   const int fi = sh.f_i, li = sh.l_i;
   const bool one_pass = S <= (int)blockDim.x && S <= kInitLens;
-  auto raw_len = [&](int i) { return one_pass ? sh.lens[i] : __ldg(prm.seq_lens + i); };
+  auto raw_len = [&](int i) { return one_pass ? sh.lens[i] : lengths.raw(i); };
   const int fL = fi >= 0 ? clamp_len(raw_len(fi), cap) : 0;
   const int fLn = fi >= 0 && fi + 1 < S ? raw_len(fi + 1) : 0;
   const int lL = li >= 0 ? clamp_len(raw_len(li), cap) : 0;
@@ -446,13 +476,15 @@ __device__ void init_walker(const DecodeParams& prm, SchedShared& sh, SegmentWal
 // starting from sequence *i at work offset *base (all lanes hold the same
 // cursor, which only moves forward). On success the cursor points at it and
 // *L is its clamped length; returns false if x lies past the last sequence.
+template <bool RAG>
 __device__ __forceinline__ bool warp_find_seq(const DecodeParams& prm, int64_t x, int& i,
                                               int64_t& base, int& L) {
+  const Lengths<RAG> lengths = lengths_of<RAG>(prm);
   const int lane = threadIdx.x & 31;
   const int S = prm.num_seqs, Hkv = prm.num_kv_heads, cap = prm.len_cap, cost = prm.unit_cost;
   while (i < S) {
     const int idx = i + lane;
-    const int Li = idx < S ? clamp_len(__ldg(prm.seq_lens + idx), cap) : 0;
+    const int Li = idx < S ? clamp_len(lengths.raw(idx), cap) : 0;
     const int64_t wi = (int64_t)Hkv * unit_work(Li, cost, prm.unit_round);
     int64_t incl = wi;
 #pragma unroll
@@ -477,16 +509,17 @@ __device__ __forceinline__ bool warp_find_seq(const DecodeParams& prm, int64_t x
 
 // Warp-wide: sets up `w` (whose constant fields are already set) for range r,
 // moving the cursor (ci, cbase) forward. Returns false for an empty range.
-__device__ __forceinline__ bool warp_start_range(const DecodeParams& prm, SegmentWalker& w,
+template <bool RAG>
+__device__ __forceinline__ bool warp_start_range(const DecodeParams& prm, SegmentWalkerOf<RAG>& w,
                                                  int64_t r, int& ci, int64_t& cbase) {
   const int64_t lo = w.cuts.lo(r), hi = w.cuts.lo(r + 1);
   if (lo >= hi) return false;
   int L = 0;
-  if (!warp_find_seq(prm, lo, ci, cbase, L)) return false;
+  if (!warp_find_seq<RAG>(prm, lo, ci, cbase, L)) return false;
   int li = ci, lL = L;
   int64_t lbase = cbase;
-  warp_find_seq(prm, hi - 1, li, lbase, lL);
-  const int fLn = ci + 1 < w.S ? __ldg(prm.seq_lens + ci + 1) : 0;
+  warp_find_seq<RAG>(prm, hi - 1, li, lbase, lL);
+  const int fLn = ci + 1 < w.S ? w.raw(ci + 1) : 0;
   start_range(w, lo, hi, ci, cbase, L, fLn, li, lbase, lL);
   return !w.done || w.tail_pending;
 }
