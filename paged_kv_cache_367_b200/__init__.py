@@ -477,7 +477,11 @@ def paged_cross_attention(out, query, k_cache, v_cache, block_table, seq_lens, q
     S, mbps = block_table.shape
     if block_table.dtype != torch.int32 or not block_table.is_contiguous():
         raise ValueError("block_table is not a contiguous int32 tensor")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws_bytes = workspace.numel() * workspace.element_size()
     _call("paged_cross_attention",
           (query, out, k_cache, v_cache, block_table, seq_lens, query_start, k_scale, v_scale,
            workspace),

@@ -113,3 +113,17 @@ def test_binding_refuses_what_the_pointers_cannot_say(lib):
         call(query_start=qs[:2])
     with pytest.raises(TypeError):
         call(k_scale=torch.ones(1, dtype=torch.float16))
+
+
+def test_binding_refuses_a_workspace_that_is_not_dense(lib):
+    """Its bytes are counted from its elements: a broadcast one holds fewer."""
+    bf = torch.bfloat16
+    q = torch.zeros(4, 8, 64, dtype=bf)
+    pool = torch.zeros(6, 16, 2, 64, dtype=bf)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30),
+               torch.zeros(64, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            pkv.paged_cross_attention(q, q, pool, pool, torch.zeros(2, 3, dtype=torch.int32),
+                                      torch.zeros(2, dtype=torch.int32),
+                                      torch.zeros(3, dtype=torch.int32), max_q_len=2,
+                                      max_seq_len=48, scale=0.1, workspace=ws, stream=0)
