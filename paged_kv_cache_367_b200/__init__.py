@@ -231,17 +231,25 @@ def pkv_rotary_inv_freq(rot_dim, *, base=10000.0, scaling=PKV_ROTARY_SCALE_NONE,
     of each pair, an fp64 tensor on `device` (default: the host), and the factor
     its outputs are multiplied by; see pkv_rotary_inv_freq in include/pagedkv.h.
     `high` defaults to 32 turns for PKV_ROTARY_SCALE_RAMP, else 4."""
+    rot_dim = _int32("rot_dim", rot_dim)
     if high is None:
         high = 32.0 if scaling == PKV_ROTARY_SCALE_RAMP else 4.0
-    freq = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    freq = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float64)
     m = ctypes.c_float()
     st = load_library().pkv_rotary_inv_freq(freq.data_ptr() if freq.numel() else None,
-                                            ctypes.addressof(m), int(rot_dim), float(base),
+                                            ctypes.addressof(m), rot_dim, float(base),
                                             int(scaling), float(factor), float(trained_len),
                                             float(low), float(high))
     if st != 0:
         raise PagedKVError("pkv_rotary_inv_freq", st)
     return (freq if device is None else freq.to(device)), m.value
+
+
+def _int32(name, n) -> int:
+    """A size as the library takes it: ctypes would drop the upper bits of a larger one."""
+    if -(1 << 31) <= n < 1 << 31:
+        return int(n)
+    raise ValueError(f"{name} {n} does not fit 32 bits")
 
 
 def _token_stride(name, t, shape, dtype):
@@ -327,6 +335,7 @@ def pkv_rotary(q_out, query, positions, inv_freq, *, k_out=None, key=None, magni
     if x is None:
         raise ValueError("neither query nor key")
     T, _, D = x.shape
+    _int32("the number of tokens", T)
     Hq = Hkv = qs = qos = ks = kos = 0
     if query is not None:
         Hq = query.shape[1]
@@ -355,6 +364,7 @@ def paged_kv_append_rotary(q_out, query, key, value, k_cache, v_cache, slot_mapp
         raise ValueError("query goes with q_out")
     rows = key.shape
     T, Hkv, D = rows
+    _int32("the number of tokens", T)
     dt = key.dtype
     ks = _token_stride("key", key, rows, dt)
     vs = _token_stride("value", value, rows, dt)
@@ -456,9 +466,11 @@ def paged_cross_attention_workspace_size(num_seqs, num_q_tokens, max_q_len, num_
                                          num_kv_heads, head_dim, max_seq_len,
                                          cache_dtype) -> int:
     """Bytes for these sizes; cache_dtype is the pool's (a torch dtype)."""
+    sizes = dict(num_seqs=num_seqs, num_q_tokens=num_q_tokens, max_q_len=max_q_len,
+                 num_heads=num_heads, num_kv_heads=num_kv_heads, head_dim=head_dim,
+                 max_seq_len=max_seq_len)
     return load_library().paged_cross_attention_workspace_size(
-        num_seqs, num_q_tokens, max_q_len, num_heads, num_kv_heads, head_dim, max_seq_len,
-        _DTYPE_CODES[cache_dtype])
+        *(_int32(k, n) for k, n in sizes.items()), _DTYPE_CODES[cache_dtype])
 
 
 def paged_cross_attention(out, query, k_cache, v_cache, block_table, seq_lens, query_start, *,
@@ -468,6 +480,9 @@ def paged_cross_attention(out, query, k_cache, v_cache, block_table, seq_lens, q
     query_start[i+1]-1 of query) over all its seq_lens[i] cached tokens; see
     paged_cross_attention in include/pagedkv.h."""
     T, Hq, D = query.shape
+    for name, n in (("the number of query tokens", T), ("max_q_len", max_q_len),
+                    ("max_seq_len", max_seq_len)):
+        _int32(name, n)
     dt = query.dtype
     if out.shape != query.shape or out.dtype != dt:
         raise ValueError("out and query differ in shape or type")

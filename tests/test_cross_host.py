@@ -127,3 +127,28 @@ def test_binding_refuses_a_workspace_that_is_not_dense(lib):
                                       torch.zeros(2, dtype=torch.int32),
                                       torch.zeros(3, dtype=torch.int32), max_q_len=2,
                                       max_seq_len=48, scale=0.1, workspace=ws, stream=0)
+
+
+@pytest.mark.parametrize("big", [1 << 32, (1 << 32) + 5, 1 << 31, -(1 << 31) - 1])
+def test_binding_refuses_sizes_past_32_bits(lib, big):
+    """They would reach the library without their upper bits (a length bound of 2^32
+    as 0)."""
+    bf = torch.bfloat16
+    q = torch.zeros(4, 8, 64, dtype=bf)
+    pool = torch.zeros(6, 16, 2, 64, dtype=bf)
+    for kw in (dict(max_q_len=big, max_seq_len=48), dict(max_q_len=2, max_seq_len=big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.paged_cross_attention(q, q, pool, pool, torch.zeros(2, 3, dtype=torch.int32),
+                                      torch.zeros(2, dtype=torch.int32),
+                                      torch.zeros(3, dtype=torch.int32), scale=0.1, stream=0, **kw)
+    sizes = (2, 10, 8, 8, 2, 128, 100)
+    for i in range(len(sizes)):
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.paged_cross_attention_workspace_size(*sizes[:i], big, *sizes[i + 1:], bf)
+    if big > 0:
+        rows = torch.zeros(1, 8, 64, dtype=bf).expand(big, 8, 64)
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.paged_cross_attention(rows, rows, pool, pool, torch.zeros(2, 3, dtype=torch.int32),
+                                      torch.zeros(2, dtype=torch.int32),
+                                      torch.zeros(3, dtype=torch.int32), max_q_len=2,
+                                      max_seq_len=48, scale=0.1, stream=0)

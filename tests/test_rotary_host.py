@@ -197,3 +197,19 @@ def test_binding_refuses_what_the_pointers_cannot_say(lib):
         app(slot_mapping=slots[:1])
     with pytest.raises(TypeError):
         app(k_scale=torch.ones(1, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("big", [1 << 31, (1 << 32) + 3])
+def test_binding_refuses_sizes_past_32_bits(lib, big):
+    """They would reach the library without their upper bits: 3 rows rotated of 2^32 + 3."""
+    D = 64
+    rows = torch.zeros(1, 2, D).expand(big, 2, D)
+    pos = torch.zeros(1, dtype=torch.int64).expand(big)
+    pool = torch.zeros(2, 8, 2, D)
+    f, _ = pkv.pkv_rotary_inv_freq(D)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.pkv_rotary(rows, rows, pos, f, stream=0)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.paged_kv_append_rotary(None, None, rows, rows, pool, pool, pos, pos, f, stream=0)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.pkv_rotary_inv_freq(big)
