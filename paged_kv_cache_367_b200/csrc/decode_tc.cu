@@ -1174,21 +1174,20 @@ static cudaError_t launch_tc_d(const DecodeParams& prm, const CUtensorMap& mk,
 }
 
 // Cross attention of at most 16 rows per unit (8: one 8-row tile), with the decode's
-// stages and residency.
-template <typename T, int D, bool F8>
-static cudaError_t launch_few_d(const DecodeParams& prm, const CUtensorMap& mk,
+// stages and residency. head_dim 128 only: at 64 the tcgen05 kernel is the faster one.
+template <typename T, bool F8>
+static cudaError_t launch_few_t(const DecodeParams& prm, const CUtensorMap& mk,
                                 const CUtensorMap& mv, int num_sms, cudaStream_t stream) {
-  constexpr int kNS = F8 ? 4 : (D == 128 ? 2 : 4);
   if (prm.rows <= 8)
-    return launch_tc_t<T, D, 1, kNS, 2, F8, 0, true>(prm, mk, mv, 0, num_sms, false, stream);
-  if constexpr (D == 64 || F8)
-    return launch_tc_t<T, D, 2, 4, 2, F8, 0, true>(prm, mk, mv, 0, num_sms, false, stream);
-  else
-    return launch_tc_t<T, D, 2, 4, 1, F8, 0, true>(prm, mk, mv, 0, num_sms, false, stream);
+    return launch_tc_t<T, 128, 1, F8 ? 4 : 2, 2, F8, 0, true>(prm, mk, mv, 0, num_sms, false,
+                                                              stream);
+  return launch_tc_t<T, 128, 2, 4, F8 ? 2 : 1, F8, 0, true>(prm, mk, mv, 0, num_sms, false,
+                                                            stream);
 }
 
 cudaError_t launch_cross_few(const DecodeParams& prm, int q_dtype, int cache_dtype, int num_sms,
                              cudaStream_t stream) {
+  if (prm.head_dim != 128 || prm.rows > 16) return cudaErrorInvalidValue;
   const bool f8 = cache_dtype == PKV_FP8_E4M3, bf16 = q_dtype == PKV_BF16;
   const CUtensorMapDataType dt = f8     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -1200,13 +1199,10 @@ cudaError_t launch_cross_few(const DecodeParams& prm, int q_dtype, int cache_dty
                        prm.num_kv_heads, prm.num_blocks))
     return cudaErrorInvalidValue;
   if (f8)
-    return bf16 ? launch_few_d<__nv_bfloat16, 128, true>(prm, mk, mv, num_sms, stream)
-                : launch_few_d<__half, 128, true>(prm, mk, mv, num_sms, stream);
-  if (prm.head_dim == 128)
-    return bf16 ? launch_few_d<__nv_bfloat16, 128, false>(prm, mk, mv, num_sms, stream)
-                : launch_few_d<__half, 128, false>(prm, mk, mv, num_sms, stream);
-  return bf16 ? launch_few_d<__nv_bfloat16, 64, false>(prm, mk, mv, num_sms, stream)
-              : launch_few_d<__half, 64, false>(prm, mk, mv, num_sms, stream);
+    return bf16 ? launch_few_t<__nv_bfloat16, true>(prm, mk, mv, num_sms, stream)
+                : launch_few_t<__half, true>(prm, mk, mv, num_sms, stream);
+  return bf16 ? launch_few_t<__nv_bfloat16, false>(prm, mk, mv, num_sms, stream)
+              : launch_few_t<__half, false>(prm, mk, mv, num_sms, stream);
 }
 
 cudaError_t launch_decode_tc(const DecodeParams& prm, int q_dtype, int cache_dtype, int max_ctas,
