@@ -172,7 +172,7 @@ int pkv_rotary_inv_freq(double* inv_freq, float* magnitude, int rot_dim, double 
  *                 may be slices of a wider tensor
  *   key, k_out    the same with num_kv_heads heads, k_stride and k_out_stride
  *   positions     [num_tokens] int64, device; any value, negative ones too. The
- *                 angle is good to |p| * 2^-52 turns per unit of inv_freq
+ *                 angle is off by at most 2^-26 + |p * inv_freq| * 2^-53 turns
  *   inv_freq      [rot_dim / 2] fp64, device: radians per position
  *
  * q_out may be query and k_out key (the same pointer and stride); other overlaps

@@ -86,7 +86,8 @@ struct RotaryParams {
   float magnitude;        // m
   float sin_sign;         // -1: transposed
   int head_dim, rot_dim, tasks, rows_per_pass;
-  Div by_heads, by_tasks, by_half;  // n: < heads + 512 rows, < 256 threads, < table entries
+  // Of n < heads + 768 rows (3 passes of 256), < 256 threads, < 6,144 table entries.
+  Div by_heads, by_tasks, by_half;
   int early;              // dependent kernels may start: only the pools are written
 };
 
@@ -388,6 +389,9 @@ cudaError_t launch_vec(RotaryParams p, cudaStream_t stream) {
   // types (64 q, 8 k/v heads of 128, 8192 tokens: 48.1 us; two take 51.9) and two of
   // fp32 (32/8 heads: 51.9 us; three take 65.8).
   constexpr int kU = sizeof(T) == 4 ? 2 : 3;
+  // The table: at most a token per row, kThreads / tasks rows a pass, tasks >= head_dim /
+  // (2 VEC), rot_dim <= head_dim. One head of 16, 32 or 512 elements fills all of it.
+  static_assert(kThreads * 2 * VEC * kU * sizeof(float) <= 48 << 10, "table without opt-in");
   if (passes <= 148 * 8) return launch(rotary_kernel<T, MODE, INTER, VEC, 1>, 1);
   return launch(rotary_kernel<T, MODE, INTER, VEC, kU>, kU);
 }

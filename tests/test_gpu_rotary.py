@@ -402,3 +402,40 @@ def test_step_on_a_rotated_cache(cuda_dev, early):
         assert_rotated(rows_, wk, size, m, "bf16")
         step()
         assert torch.equal(out, got)
+
+
+@pytest.mark.parametrize("D", [16, 32, 512])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotary_one_head_at_many_positions(cuda_dev, D, inter):
+    """A block of as many tokens as it can hold: its table of cosines and sines takes
+    all of the shared memory that needs no opt-in."""
+    T = 148 * 8 * (4096 // D) + 777
+    gen = torch.Generator(device=cuda_dev).manual_seed(D)
+    q = torch.randn((T, 1, D), generator=gen, device=cuda_dev).to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (T,), generator=gen, device=cuda_dev)
+    f, _ = pkv.pkv_rotary_inv_freq(D, device=cuda_dev)
+    out = torch.full_like(q, float("nan"))
+    pkv.pkv_rotary(out, q, pos, f, flags=pkv.PKV_ROTARY_INTERLEAVED if inter else 0)
+    assert torch.isfinite(out).all()
+    some = torch.cat([torch.arange(800), torch.randint(0, T, (4000,)), torch.arange(T - 800, T)]).cuda()
+    want, size = formula(q[some], pos[some], f, 1.0, inter, False)
+    assert_rotated(out[some], want, size, 1.0, "bf16")
+
+
+@pytest.mark.parametrize("p", [1, 3, 1000, (1 << 20) + 1, 1 << 40, -(1 << 52)])
+def test_rotary_angle_bound(cuda_dev, p):
+    """The stated bound of the angle, 2^-26 + |p f| 2^-53 turns, in fp32: a unit vector
+    moves by 2 pi times that, and by three fp32 steps of sine, cosine and products."""
+    f, _ = pkv.pkv_rotary_inv_freq(64, device=cuda_dev)
+    x = torch.zeros((1, 1, 64), device=cuda_dev)
+    x[..., :32] = 1.0
+    out = torch.empty_like(x)
+    pkv.pkv_rotary(out, x, torch.tensor([p], device=cuda_dev), f)
+    with_f = f.cpu().numpy().astype(np.longdouble)
+    t = np.asarray([p], np.longdouble) * with_f
+    bound = 2 * np.pi * (2.0 ** -26 + np.abs(t) * 2.0 ** -53) + 3 * 2.0 ** -23
+    # The reference's own reduction: a 64-bit mantissa of |t|.
+    bound += np.abs(t) * 2.0 ** -63
+    got = out.cpu().numpy().astype(np.longdouble)[0, 0]
+    assert (np.abs(got[:32] - np.cos(t)) <= bound).all()
+    assert (np.abs(got[32:] - np.sin(t)) <= bound).all()
