@@ -48,8 +48,9 @@ namespace {
 // warp has eight parts in flight, their log-sum-exps and rows together (a running
 // maximum rescales the sums), so a row of up to eight costs one memory latency; a row
 // of more is given a block of its own (one warp for each of 448 rows of 296 parts took
-// 60 us). Launched before the main kernel has ended (programmatic dependent launch); it
-// finds its row meanwhile.
+// 60 us). A programmatic dependent launch: the main kernel triggers it only by its CTAs'
+// ends, so what overlaps is the launch and the search for the row with the last CTAs'
+// writes becoming visible.
 constexpr int kJoinWarps = 8;
 template <typename OT, int D, int kWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PrefillParams p) {

@@ -487,7 +487,7 @@ __device__ __forceinline__ int take_next_cta(uint4* answer, uint64_t* bar, uint3
 // The items of this CTA, as the producer publishes them in a ring of kRing
 // records, and their chunks, in order. Every role walks the same sequence, so
 // the position of a chunk in it (its index j) names the same K/V stage
-// (j % kNS), S buffer (j % 2) and barrier phases in every role. All lanes of a
+// (j % kNSx), S buffer (j % kBufs) and barrier phases in every role. All lanes of a
 // warp call the methods; a record with no chunks ends the sequence.
 template <typename T>
 struct Walk {
@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(Cfg5<D, F8, KIND>::kThreads,
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait5(bar, parity, abort));
     };
-    auto issue_s = [&](int j) {  // S_t(j) = Q_t K(j)^T into buffer j % 2
+    auto issue_s = [&](int j) {  // S_t(j) = Q_t K(j)^T into buffer j % kBufs
       // Base descriptors once; the K steps add compile-time offsets to the
       // 14-bit address field (addresses stay below 256 KB, so it never carries).
       const uint64_t a0 = sdesc(q_addr + t * C::kQ, 16);
