@@ -572,7 +572,9 @@ int paged_kv_append_rotary(void* q_out, const void* query, const void* key, cons
     return PKV_ERR_NULL;
   if (!rot::aligned(q_out, 16) || !rot::aligned(query, 16) || !rot::aligned(key, 16) ||
       !rot::aligned(value, 16) || !rot::aligned(k_cache, 16) || !rot::aligned(v_cache, 16) ||
-      !rot::aligned(slot_mapping, 8) || !rot::aligned(positions, 8) || !rot::aligned(inv_freq, 8))
+      !rot::aligned(slot_mapping, 8) || !rot::aligned(positions, 8) ||
+      !rot::aligned(inv_freq, 8) ||
+      (fp8 && (!rot::aligned(k_scale, 4) || !rot::aligned(v_scale, 4))))
     return PKV_ERR_ALIGN;
   p.dst[1] = k_cache, p.dst[2] = v_cache;
   p.end[0] = num_heads, p.end[1] = num_heads + num_kv_heads, p.end[2] = p.end[1] + num_kv_heads;

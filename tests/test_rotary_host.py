@@ -213,3 +213,8 @@ def test_binding_refuses_sizes_past_32_bits(lib, big):
         pkv.paged_kv_append_rotary(None, None, rows, rows, pool, pool, pos, pos, f, stream=0)
     with pytest.raises(ValueError, match="32 bits"):
         pkv.pkv_rotary_inv_freq(big)
+
+
+@pytest.mark.parametrize("scale", ["k_scale", "v_scale"])
+def test_append_rotary_rejects_a_misaligned_scale(lib, scale):
+    assert append_rotary(lib, cache_dtype=FP8, **{scale: A + 2}) == EALIGN
