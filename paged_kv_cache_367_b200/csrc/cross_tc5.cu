@@ -21,7 +21,9 @@
 // 60,000-65,536 E4M3 tokens 86 us (0.47 of the HBM rate: a chain of widening, S, softmax
 // and PV of 1,250 clocks per 64-token chunk); 64 x 1 query over 16-2,048 tokens 62 us
 // (0.75); 8 x 5 queries of 16 heads of 64 over 1,500 tokens 17 us; one query over 4,096
-// tokens 13 us.
+// tokens 13 us; 16 x 10, 16 and 32 queries of 32/8 heads over 2,000-4,096 tokens (two
+// copies of the rows, two, one) 56, 59 and 61 us; 2 x 300 of them over 8,192, 80 units
+// uncut on 148 SMs, 157 us (513 TFLOP/s).
 //
 // Items are handed out through cluster launch control (a CTA per item in the grid;
 // running CTAs take over those not yet launched), so a call keeps no counter in
